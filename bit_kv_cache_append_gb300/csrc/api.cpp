@@ -583,6 +583,8 @@ kv_status plan_multi(const kv_cache* c, int layer, const void* q, int n_queries,
   a.k_unit = std::ldexp(1.0f, -kvq::multi_unit_shift(g.kb));
   a.v_unit = std::ldexp(1.0f, -kvq::multi_unit_shift(g.vb));
   a.v_scale = 1.0f / a.v_unit;
+  // (the bf16 below 2^16 is 65280, which f16 rounds to a finite value)
+  a.v_top = g.act_bf16 ? (127u + 16u + kvq::multi_unit_shift(g.vb)) << 7 : 0x7c00u;
   a.qscale = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(g.D))) / a.k_unit;
   const int64_t per_unit = static_cast<int64_t>(a.n_groups) + (a.n_sink > 0) + a.tail_blocks + a.draft_blocks;
   a.lens = lens;

@@ -155,6 +155,7 @@ struct MultiAttnArgs {
   float qscale;           // log2(e) / sqrt(D) / k_unit
   float k_unit, v_unit;   // keys and values are held times these (powers of two)
   float v_scale;          // 1 / v_unit
+  uint32_t v_top;         // bits of the least activation that times v_unit is not finite in f16
 };
 // CTAs of the split kernel for a call of this many blocks (at most).
 int multi_attn_ctas(int64_t units, int64_t blocks, bool wide, bool ragged, int sm_count);

@@ -580,9 +580,9 @@ __device__ __forceinline__ void exact_keys_at_once(const MultiAttnArgs& a, int b
 // Values of an exact block and channel group vg: put as group_values; columns
 // outside `cols` are zero. A lane loads a channel pair of every eighth row,
 // and eight rows by eight channels are transposed at a time. In a draft block
-// a value that is not finite is put as zero too, so that it cannot meet the
-// zero weight of a row that does not see it; returns the columns that had one
-// (in every lane).
+// a value that is not finite in f16 (a bf16 value from 65536 / v_unit on among
+// them) is put as zero too, so that it cannot meet the zero weight of a row
+// that does not see it; returns the columns that had one (in every lane).
 template <int D, class Put>
 __device__ __forceinline__ uint32_t exact_values(const MultiAttnArgs& a, int b, int h, int kind, int idx, int vg,
                                                  uint32_t cols, int lane, Put put) {
@@ -601,13 +601,13 @@ __device__ __forceinline__ uint32_t exact_values(const MultiAttnArgs& a, int b, 
   }
   uint32_t bad = 0;
   if (kind == kDraftBlock) {
-    const uint32_t top = bf ? 0x7f80u : 0x7c00u;
+    const uint32_t top = a.v_top;
 #pragma unroll
     for (int k = 0; k < 4; ++k)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        if ((x[k][i] & top) == top) x[k][i] &= 0xffff0000u, bad |= 1u << (8 * k + g);
-        if ((x[k][i] & top << 16) == top << 16) x[k][i] &= 0x0000ffffu, bad |= 1u << (8 * k + g);
+        if ((x[k][i] & 0x7fffu) >= top) x[k][i] &= 0xffff0000u, bad |= 1u << (8 * k + g);
+        if ((x[k][i] & 0x7fff0000u) >= top << 16) x[k][i] &= 0x0000ffffu, bad |= 1u << (8 * k + g);
       }
   }
   __syncwarp();
@@ -648,7 +648,7 @@ __device__ __forceinline__ void block_keys(const MultiAttnArgs& a, const Segment
 // Values of channel group vg of NB blocks from blk on, put(block, m-tile of
 // the two, 8 words); `src`: the blocks' chunks, where they are groups. Columns
 // that do not count are zero. Draft blocks' columns that held a value that is
-// not finite go to bad[].
+// not finite in f16 go to bad[].
 template <int D, int VB, int NB, class Put>
 __device__ __forceinline__ void block_values(const MultiAttnArgs& a, const SegmentCursor& seg, int blk, const uint8_t* src,
                                              int vg, int lane, uint32_t* bad, Put put) {

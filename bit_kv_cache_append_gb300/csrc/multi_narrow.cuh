@@ -107,7 +107,7 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
   uint64_t *s_full = k_full + 15, *s_empty = k_full + 19;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + T::OFF_MISC);
   uint32_t* tmem_at = reinterpret_cast<uint32_t*>(smem + T::OFF_MISC + 4);
-  // columns of segment i's draft block k with a value that is not finite:
+  // columns of segment i's draft block k with a value that is not finite in f16:
   // bad[8 (i & 7) + k]. The value warps write it and clear the place of
   // segment i + 3 when they begin segment i: they are never more than two
   // tiles apart, nor more than two ahead of what the softmax warps read.
@@ -362,11 +362,13 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
             for (uint32_t left = bad[8 * (n_seg & 7) + k]; left; left &= left - 1) {
               const int j = __ffs(left) - 1;
               const size_t at = ((static_cast<size_t>(b) * a.geo.H + h) * a.T + kGroup * k + j) * D + col;
-              const float x = act_to_float(a.vd[at], a.geo.act_bf16);
+              const uint16_t x = a.vd[at];
+              if ((x & 0x7fffu) < a.v_top) continue;
 #pragma unroll
               for (int i = 0; i < 8; ++i) {
                 const int r = n + i;
-                if (!(fabsf(x) < INFINITY) && r < a.rows && (draft_bits(a, b, r % a.T, k) >> j & 1u)) o[i] += x;
+                if (r < a.rows && (draft_bits(a, b, r % a.T, k) >> j & 1u))
+                  o[i] = fmaf(act_to_float(x, a.geo.act_bf16), INFINITY, o[i]);
               }
             }
           }

@@ -111,7 +111,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
   uint64_t *p_full = k_full + 10, *o_done = k_full + 12, *q_full = k_full + 14, *drain = k_full + 15;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(rest + T::MISC);
   uint32_t* tmem_at = reinterpret_cast<uint32_t*>(rest + T::MISC + 4);
-  // columns of segment i's draft blocks with a value that is not finite, as in
+  // columns of segment i's draft blocks with a value that is not finite in f16, as in
   // multi_narrow.cuh: bad[8 (i & 7) + block], cleared three segments ahead
   uint32_t* bad = reinterpret_cast<uint32_t*>(rest + T::MISC + 16);
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -348,10 +348,8 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                 const uint16_t* v =
                     a.vd + ((static_cast<size_t>(b) * a.geo.H + h) * a.T + kGroup * k + __ffs(left) - 1) * D + n;
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                  const float x = act_to_float(v[j], a.geo.act_bf16);
-                  if (!(fabsf(x) < INFINITY)) o[j] += x;
-                }
+                for (int j = 0; j < 8; ++j)
+                  if ((v[j] & 0x7fffu) >= a.v_top) o[j] = fmaf(act_to_float(v[j], a.geo.act_bf16), INFINITY, o[j]);
               }
             }
             if (whole) {

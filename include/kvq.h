@@ -292,9 +292,10 @@ kv_status kv_attn_workspace_bytes(const kv_cache* cache, int n_queries, size_t* 
  * j % 64 of word j / 64 of row i is set where token i sees drafted token j
  * (itself included; bits at and above n_draft are ignored). A tree's mask is
  * each token's ancestors and itself; any other mask is computed as given.
- * What a value row holds that no token sees, or the weight of a token that
- * does not see it, takes no part in a result, whatever it is (NaN and
- * infinity too). When the cache applies RoPE, drafted token i is
+ * What a value row holds takes no part in the results of tokens that do not
+ * see it, whatever it is (NaN and infinity too). A bf16 value beyond f16's
+ * range (from 65536 on; 2^17 and 2^19 with 2- and 3-bit V codes) is an
+ * infinity to the tokens that see it. When the cache applies RoPE, drafted token i is
  * at position L + s - 1 with s the number of drafted tokens it sees (L for
  * s = 0): q row i and k_draft row i are rotated there, the key rounded to
  * act_dtype as kv_append would; KV_ERR_CAPACITY when L + n_draft exceeds
