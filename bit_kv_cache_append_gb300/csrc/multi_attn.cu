@@ -90,11 +90,14 @@ __global__ void __launch_bounds__(kMultiMergeWarps * 32, 4)
 #pragma unroll
     for (int k = 0; k < NC; ++k) o[k] = 0.0f;
     auto add = [&](float m, float sum, const float (&x)[NC], float ref) {
-      // (a partial that saw nothing has weight zero; a NaN in one stays one)
-      const float w = m == -INFINITY && sum == 0.0f ? 0.0f : fast_exp2(m - ref);
-      l = w == 0.0f ? l : fmaf(sum, w, l);
+      // A partial that saw nothing takes no part. One that did does with any
+      // weight, zero too: where all its scores were NaN its maximum is -inf,
+      // and its sum is what carries the NaN.
+      const bool none = m == -INFINITY && sum == 0.0f;
+      const float w = none ? 0.0f : fast_exp2(m - ref);
+      l = fmaf(sum, w, l);
 #pragma unroll
-      for (int k = 0; k < NC; ++k) o[k] = w == 0.0f ? o[k] : fmaf(x[k], w, o[k]);
+      for (int k = 0; k < NC; ++k) o[k] = none ? o[k] : fmaf(x[k], w, o[k]);
     };
     auto rescale = [&](float top) {  // to the larger maximum; returns what weights are taken against
       const float now = fmaxf(M, top), ref = now == -INFINITY ? 0.0f : now;
