@@ -33,7 +33,7 @@ SYMBOLS = ("kv_cache_required_bytes", "kv_cache_create", "kv_cache_destroy", "kv
            "kv_cache_set_timing_events", "kv_launch_count", "kv_copy_bandwidth_kernel",
            "kv_last_error", "kv_decode_attn_noalloc", "kv_cache_test_bounded_wait",
            "kv_attn_workspace_bytes", "kv_tree_attn", "kv_cross_attn", "kv_rope_create", "kv_rope_destroy",
-           "kv_rope_apply", "kv_qk_norm_rope")
+           "kv_rope_apply", "kv_qk_norm_rope", "kv_attn_test_bounded_wait")
 
 
 class KVError(RuntimeError):
@@ -92,6 +92,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "kv_cache_export": [vp, i32, i32, vp, sz, vp],
         "kv_cache_check_device_error": [vp, vp],
         "kv_cache_test_bounded_wait": [vp, i64, ctypes.POINTER(i64), vp],
+        "kv_attn_test_bounded_wait": [vp, i64, ctypes.POINTER(i64), vp],
         "kv_cache_set_timing_events": [vp, vp, vp],
         "kv_copy_bandwidth_kernel": [vp, vp, sz, vp],
         "kv_attn_workspace_bytes": [vp, i32, ctypes.POINTER(sz)],
@@ -422,6 +423,13 @@ class KVCache:
         returns the 5 result words (see kvq.h)."""
         res = (ctypes.c_int64 * 5)()
         check(lib().kv_cache_test_bounded_wait(self.handle, int(budget_cycles), res, _stream_ptr(stream)))
+        return [int(x) for x in res]
+
+    def test_attn_bounded_wait(self, budget_cycles, stream=None):
+        """kv_attn_test_bounded_wait: the same of the waits of tree_attn and
+        cross_attn; returns the 8 result words (see kvq.h)."""
+        res = (ctypes.c_int64 * 8)()
+        check(lib().kv_attn_test_bounded_wait(self.handle, int(budget_cycles), res, _stream_ptr(stream)))
         return [int(x) for x in res]
 
     def set_timing_events(self, ev_begin, ev_end):

@@ -1002,25 +1002,41 @@ kv_status kv_cache_set_timing_events(kv_cache* cache, void* ev_begin, void* ev_e
   return KV_OK;
 }
 
-kv_status kv_cache_test_bounded_wait(kv_cache* cache, int64_t budget_cycles, int64_t* host_result,
-                                     void* cuda_stream) {
+namespace {
+
+// One launch of a wait probe; its n results go through the arena's error
+// block, after the flag.
+kv_status run_wait_probe(kv_cache* cache, int64_t budget_cycles, int64_t* host_result, int n, void* cuda_stream,
+                         cudaError_t (*launch)(int*, long long*, long long, cudaStream_t, int64_t*), const char* what) {
   if (!cache) return fail(KV_ERR_INVALID_ARG, "cache is NULL");
   if (!host_result) return fail(KV_ERR_INVALID_ARG, "host_result is NULL");
   if (budget_cycles < 1000 || budget_cycles > (int64_t{1} << 31))
     return fail(KV_ERR_INVALID_ARG, "budget_cycles must be in [1000, 2^31]");
   cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
-  // the results go to the arena's error block, after the flag
   long long* res = reinterpret_cast<long long*>(cache->arena + cache->geo.off_err + 64);
   int64_t launches = 0;
-  cudaError_t e = cudaMemsetAsync(res, 0xff, 5 * sizeof(long long), s);
+  cudaError_t e = cudaMemsetAsync(res, 0xff, n * sizeof(long long), s);
   if (e == cudaSuccess)
-    e = kvq::launch_wait_probe(reinterpret_cast<int*>(cache->arena + cache->geo.off_err), res, budget_cycles, s,
-                               &launches);
+    e = launch(reinterpret_cast<int*>(cache->arena + cache->geo.off_err), res, budget_cycles, s, &launches);
   g_launches += launches;
   if (e == cudaSuccess) e = cudaStreamSynchronize(s);
-  if (e == cudaSuccess) e = cudaMemcpy(host_result, res, 5 * sizeof(long long), cudaMemcpyDeviceToHost);
-  if (e != cudaSuccess) return cuda_fail(e, "kv_cache_test_bounded_wait");
+  if (e == cudaSuccess) e = cudaMemcpy(host_result, res, n * sizeof(long long), cudaMemcpyDeviceToHost);
+  if (e != cudaSuccess) return cuda_fail(e, what);
   return KV_OK;
+}
+
+}  // namespace
+
+kv_status kv_cache_test_bounded_wait(kv_cache* cache, int64_t budget_cycles, int64_t* host_result,
+                                     void* cuda_stream) {
+  return run_wait_probe(cache, budget_cycles, host_result, 5, cuda_stream, kvq::launch_wait_probe,
+                        "kv_cache_test_bounded_wait");
+}
+
+kv_status kv_attn_test_bounded_wait(kv_cache* cache, int64_t budget_cycles, int64_t* host_result,
+                                    void* cuda_stream) {
+  return run_wait_probe(cache, budget_cycles, host_result, 8, cuda_stream, kvq::launch_multi_wait_probe,
+                        "kv_attn_test_bounded_wait");
 }
 
 int64_t kv_launch_count(void) { return g_launches.load(); }

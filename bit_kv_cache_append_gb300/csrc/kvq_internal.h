@@ -166,6 +166,10 @@ int multi_unit_shift(int bits);
 int multi_tile_rows(int rows);
 int multi_seg_cost(int tile_rows);
 cudaError_t launch_multi_attn(MultiAttnArgs& a, cudaStream_t s, int64_t* launches);
+// The split kernels' bounded waits run out on barriers nobody completes (res: 8
+// device int64).
+cudaError_t launch_multi_wait_probe(int* err_flag, long long* res, long long budget, cudaStream_t s,
+                                    int64_t* launches);
 
 // Device ordinal the cache was created on.
 int cache_device(const kv_cache* cache);

@@ -216,6 +216,35 @@ cudaError_t launch_d(const MultiAttnArgs& a, cudaStream_t s, int64_t* launches) 
   return cudaSuccess;
 }
 
+// The split kernels' waits made to run out, as wait_probe_kernel does with the
+// decode's: four barriers that nothing arrives at. Warp 0 (pipe_wait) gives up
+// after `budget` cycles, warp 2 (pipe_wait_short) after kProbeRounds rounds, and
+// both raise an abort flag; warps 1 and 3 wait with the kernels' own bounds and
+// must leave through that flag. res[w]: 1 if warp w's wait returned "completed"
+// (must be 0), res[4 + w]: the SM clock cycles it took.
+constexpr int kProbeRounds = 8;
+__global__ void __launch_bounds__(128) multi_wait_probe_kernel(int* err_flag, long long* res, long long budget) {
+  __shared__ __align__(8) uint64_t bars[4];
+  __shared__ int abort_flags[2];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x < 4) mbar_init(&bars[threadIdx.x], 1);
+  if (threadIdx.x < 2) abort_flags[threadIdx.x] = 0;
+  mbar_fence_init();
+  __syncthreads();
+  volatile int* ab = &abort_flags[warp >> 1];
+  const long long t0 = clock64();
+  bool ok;
+  if (warp == 0) ok = pipe_wait(&bars[0], 0, ab, budget);
+  else if (warp == 1) ok = pipe_wait(&bars[1], 0, ab);
+  else if (warp == 2) ok = pipe_wait_short(&bars[2], 0, ab, kProbeRounds);
+  else ok = pipe_wait_short(&bars[3], 0, ab);
+  if (lane == 0) {
+    res[warp] = ok ? 1 : 0;
+    res[4 + warp] = clock64() - t0;
+    if (!ok) set_error(err_flag, kErrTimeout);
+  }
+}
+
 }  // namespace
 
 // Rows of a tile: up to 32 rows the columns are the products' long side and
@@ -247,6 +276,13 @@ int multi_attn_ctas(int64_t units, int64_t blocks, bool wide, bool ragged, int s
   if (!ragged && units <= sm_count && blocks * (sm_count - units) <= kTileBlocks * few)
     return static_cast<int>(units);
   return static_cast<int>(tiles < sm_count ? tiles : sm_count);
+}
+
+cudaError_t launch_multi_wait_probe(int* err_flag, long long* res, long long budget, cudaStream_t s,
+                                    int64_t* launches) {
+  multi_wait_probe_kernel<<<1, 128, 0, s>>>(err_flag, res, budget);
+  ++*launches;
+  return cudaGetLastError();
 }
 
 cudaError_t launch_multi_attn(MultiAttnArgs& a, cudaStream_t s, int64_t* launches) {

@@ -185,37 +185,44 @@ struct SegmentCursor {
   __device__ __forceinline__ bool plain(int blk, int n) const { return blk >= seq.plain0 && blk + n <= seq.plain1; }
 };
 
+// Up to 32 polls of phase `parity` of `bar` by a whole warp, three instructions
+// each; true once it is complete. A poll that finds it incomplete is suspended
+// until it completes, or for the hardware's own limit, 7860 cycles as
+// multi_wait_probe_kernel measures them: a round that fails takes 0.25 M cycles,
+// an eighth of a millisecond. (With a limit of a microsecond given the hardware
+// waits as long, and the ring shape takes 163 us instead of 155.)
+__device__ __forceinline__ bool pipe_poll(uint32_t bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\t"
+      "mov.u32 n, 32;\n"
+      "again:\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "@p bra over;\n\t"
+      "sub.u32 n, n, 1;\n\t"
+      "setp.ne.u32 q, n, 0;\n\t"
+      "@q bra again;\n"
+      "over:\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return __all_sync(0xffffffffu, done != 0);
+}
+
 // Wait of a whole warp for phase `parity` of `bar`, bounded and abortable as
 // warp_wait is. Many warps wait at any time here and share the schedulers with
-// those that work, so a poll is three instructions (a blocking try_wait, which
-// the hardware suspends and wakes) and the clock and the abort flag are looked
-// at once in 32: a third of all instructions were polls with warp_wait.
-__device__ __forceinline__ bool pipe_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+// those that work, so the clock and the abort flag are looked at once a round
+// of polls: a third of all instructions were polls with warp_wait.
+__device__ __forceinline__ bool pipe_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
+                                          long long budget = kWaitCycles) {
   const uint32_t addr = smem_u32(bar);
-  auto poll = [&]() {
-    uint32_t done;
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\t"
-        "mov.u32 n, 32;\n"
-        "again:\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "@p bra over;\n\t"
-        "sub.u32 n, n, 1;\n\t"
-        "setp.ne.u32 q, n, 0;\n\t"
-        "@q bra again;\n"
-        "over:\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(done)
-        : "r"(addr), "r"(parity)
-        : "memory");
-    return __all_sync(0xffffffffu, done != 0);
-  };
-  if (poll()) return true;
+  if (pipe_poll(addr, parity)) return true;
   const long long t0 = clock64();
   while (true) {
-    if (poll()) return true;
+    if (pipe_poll(addr, parity)) return true;
     if (__any_sync(0xffffffffu, *abort_flag != 0)) return false;
-    if (__any_sync(0xffffffffu, clock64() - t0 > kWaitCycles)) {
+    if (__any_sync(0xffffffffu, clock64() - t0 > budget)) {
       *abort_flag = 1;
       return false;
     }
@@ -225,27 +232,16 @@ __device__ __forceinline__ bool pipe_wait(uint64_t* bar, uint32_t parity, volati
 // The same with less code, for the kernel of 128-row tiles, whose roles do not
 // fit the instruction cache together otherwise (ring shape 208 -> 191 us, 384
 // queries 218 -> 211 us; in the other kernel batch 16 went from 202 to 219 us
-// with it): the bound is a count of polls, 32 x 2^18, about a second.
-__device__ __forceinline__ bool pipe_wait_short(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+// with it): the bound is a count of rounds, 2^13 of them 2.06 G cycles, about a
+// second. (With the clock read in every round the ring shape takes 157 us
+// instead of 155, 384 queries 187.7 instead of 186.3.)
+constexpr int kWaitRounds = 1 << 13;
+__device__ __forceinline__ bool pipe_wait_short(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
+                                                int rounds = kWaitRounds) {
   const uint32_t addr = smem_u32(bar);
 #pragma unroll 1
-  for (int i = 0; i < 1 << 18; ++i) {
-    uint32_t done;
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\t"
-        "mov.u32 n, 32;\n"
-        "again:\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "@p bra over;\n\t"
-        "sub.u32 n, n, 1;\n\t"
-        "setp.ne.u32 q, n, 0;\n\t"
-        "@q bra again;\n"
-        "over:\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(done)
-        : "r"(addr), "r"(parity)
-        : "memory");
-    if (__all_sync(0xffffffffu, done != 0)) return true;
+  for (int i = 0; i < rounds; ++i) {
+    if (pipe_poll(addr, parity)) return true;
     if (__any_sync(0xffffffffu, *abort_flag != 0)) return false;
   }
   *abort_flag = 1;

@@ -459,6 +459,16 @@ kv_status kv_cache_check_device_error(kv_cache* cache, void* cuda_stream);
 kv_status kv_cache_test_bounded_wait(kv_cache* cache, int64_t budget_cycles, int64_t* host_result,
                                      void* cuda_stream);
 
+/* The same for the two waits of kv_tree_attn and kv_cross_attn, one bounded by
+ * the clock and one by a count of rounds of polls: a warp gives up after
+ * `budget_cycles` (in [1000, 2^31]) of the one, a second after 8 rounds of the
+ * other (the kernels' own bound is 8192), and two more, with the kernels' own
+ * bounds, through the abort flags those raise. host_result receives 8 int64:
+ * per warp 1 if its wait returned "completed" (must all be 0), then the SM
+ * cycles each waited (warps 0 and 1: the first wait, 2 and 3: the second). */
+kv_status kv_attn_test_bounded_wait(kv_cache* cache, int64_t budget_cycles, int64_t* host_result,
+                                    void* cuda_stream);
+
 /* Optional timing hook: when both are non-NULL, kv_decode_attn records
  * ev_begin (a cudaEvent_t) right before its split kernel and ev_end right
  * after its merge kernel (the whole decode), on the call's stream. Pass
