@@ -10,6 +10,7 @@
 #include <cstdlib>
 #include <cstdint>
 #include <cstring>
+#include <initializer_list>
 #include <new>
 #include <string>
 #include <vector>
@@ -537,14 +538,35 @@ void plan_rows(const kv_cache* c, int n_queries, MultiPlan* p) {
   p->bytes = p->o_bytes + align256(parts * a.copies * a.tile_rows * 2 * 4);
 }
 
-bool overlap(const void* a, size_t a_bytes, const void* b, size_t b_bytes) {
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return x < y + b_bytes && y < x + a_bytes;
+// Memory that a call reads or writes; a NULL pointer is none.
+struct Range {
+  const char* name;
+  const void* at;
+  size_t bytes;
+};
+
+// CTAs write the outputs and the workspace while others still read, so what is
+// written must overlap neither what is read (lengths or a mask that change on
+// the way would also lead the merge to partials that nobody wrote) nor
+// anything else that is written.
+kv_status check_apart(const Range (&written)[3], std::initializer_list<Range> read) {
+  auto meet = [](const Range& a, const Range& b) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a.at), y = reinterpret_cast<uintptr_t>(b.at);
+    return x && y && x < y + b.bytes && y < x + a.bytes;
+  };
+  for (const Range& w : written) {
+    for (const Range& r : read)
+      if (meet(w, r)) return fail(KV_ERR_INVALID_ARG, std::string(w.name) + " must not overlap " + r.name);
+    for (const Range& v : written)
+      if (&v < &w && meet(w, v)) return fail(KV_ERR_INVALID_ARG, std::string(w.name) + " must not overlap " + v.name);
+  }
+  return KV_OK;
 }
 
 // Checks common to kv_tree_attn and kv_cross_attn, and the call's plan.
-kv_status plan_multi(const kv_cache* c, int layer, const void* q, int n_queries, int n_draft, const void* out,
-                     const int32_t* lens, const float* lse, void* workspace, size_t workspace_bytes, MultiPlan* p) {
+kv_status plan_multi(const kv_cache* c, int layer, const void* q, int n_queries, int n_draft, const void* k_draft,
+                     const void* v_draft, const uint64_t* mask, const void* out, const int32_t* lens, const float* lse,
+                     void* workspace, size_t workspace_bytes, MultiPlan* p) {
   kv_status st = check_layer(c, layer);
   if (st != KV_OK || (st = check_multi(c, n_queries)) != KV_OK) return st;
   if (!q || !out) return fail(KV_ERR_INVALID_ARG, "q/out is NULL");
@@ -557,13 +579,21 @@ kv_status plan_multi(const kv_cache* c, int layer, const void* q, int n_queries,
   if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
   if (dev != c->device) return fail(KV_ERR_INVALID_ARG, "the cache's device must be the current device");
   const Geometry& g = c->geo;
-  const size_t q_bytes = static_cast<size_t>(g.B) * g.Hq * n_queries * g.D * 2;
-  if (overlap(out, q_bytes, q, q_bytes)) return fail(KV_ERR_INVALID_ARG, "out must not overlap q");
   const LayerState& ls = c->layers[layer];
   *p = MultiPlan{};
   plan_rows(c, n_queries, p);
   if (workspace_bytes < p->bytes)
     return fail(KV_ERR_INVALID_ARG, "workspace smaller than kv_attn_workspace_bytes");
+  const size_t rows = static_cast<size_t>(g.B) * g.Hq * n_queries, q_bytes = rows * g.D * 2;
+  const size_t mask_bytes = static_cast<size_t>(g.B) * n_draft * ((static_cast<size_t>(n_draft) + 63) / 64) * 8;
+  st = check_apart({{"out", out, q_bytes}, {"lse", lse, rows * 4}, {"workspace", workspace, p->bytes}},
+                   {{"q", q, q_bytes},
+                    {"k_draft", k_draft, q_bytes / g.gqa},
+                    {"v_draft", v_draft, q_bytes / g.gqa},
+                    {"mask", mask, mask_bytes},
+                    {"lengths", lens, static_cast<size_t>(g.B) * 4},
+                    {"the cache", c->arena, g.total}});
+  if (st != KV_OK) return st;
   kvq::MultiAttnArgs& a = p->a;
   a.lay = layer_dev(c, layer);
   a.tab = tables_dev(c);
@@ -621,16 +651,14 @@ kv_status kv_tree_attn(kv_cache* cache, int layer, const void* q, const void* k_
                        int n_draft, const uint64_t* mask, void* out, float* lse_or_null, void* workspace,
                        size_t workspace_bytes, void* cuda_stream) {
   MultiPlan p;
-  kv_status st = plan_multi(cache, layer, q, n_draft, n_draft, out, nullptr, lse_or_null, workspace, workspace_bytes, &p);
+  kv_status st = plan_multi(cache, layer, q, n_draft, n_draft, k_draft, v_draft, mask, out, nullptr, lse_or_null,
+                            workspace, workspace_bytes, &p);
   if (st != KV_OK) return st;
   if (n_draft > 256) return fail(KV_ERR_UNSUPPORTED, "at most 256 drafted tokens");
   if (!k_draft || !v_draft || !mask) return fail(KV_ERR_INVALID_ARG, "k_draft, v_draft or mask is NULL");
   if (!aligned16(k_draft) || !aligned16(v_draft))
     return fail(KV_ERR_INVALID_ARG, "k_draft and v_draft must be 16-byte aligned");
   if (reinterpret_cast<uintptr_t>(mask) & 7u) return fail(KV_ERR_INVALID_ARG, "mask must be 8-byte aligned");
-  const size_t kv_bytes = static_cast<size_t>(p.a.geo.B) * p.a.geo.H * n_draft * p.a.geo.D * 2, o_bytes = kv_bytes * p.a.geo.gqa;
-  if (overlap(out, o_bytes, k_draft, kv_bytes) || overlap(out, o_bytes, v_draft, kv_bytes))
-    return fail(KV_ERR_INVALID_ARG, "out must not overlap k_draft or v_draft");
   if (p.a.geo.rope_max_pos && p.a.L + n_draft > p.a.geo.rope_max_pos)
     return fail(KV_ERR_CAPACITY, "drafted positions beyond rope_max_pos");
   p.a.kd = static_cast<const uint16_t*>(k_draft);
@@ -643,7 +671,8 @@ kv_status kv_tree_attn(kv_cache* cache, int layer, const void* q, const void* k_
 kv_status kv_cross_attn(kv_cache* cache, int layer, const void* q, int n_queries, const int32_t* lengths_or_null,
                         void* out, float* lse_or_null, void* workspace, size_t workspace_bytes, void* cuda_stream) {
   MultiPlan p;
-  kv_status st = plan_multi(cache, layer, q, n_queries, 0, out, lengths_or_null, lse_or_null, workspace, workspace_bytes, &p);
+  kv_status st = plan_multi(cache, layer, q, n_queries, 0, nullptr, nullptr, nullptr, out, lengths_or_null, lse_or_null,
+                            workspace, workspace_bytes, &p);
   if (st != KV_OK) return st;
   if (p.a.geo.rope_max_pos)
     return fail(KV_ERR_UNSUPPORTED, "cross attention has no query positions: the cache must not apply RoPE");

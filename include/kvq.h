@@ -264,12 +264,13 @@ kv_status kv_decode_attn_noalloc(kv_cache* cache, int layer, const void* q, floa
  * exact, the rest from the codes), for caches in KIVI mode with keys rotated
  * before they are stored (or by the caller) and no re-positioning; others
  * get KV_ERR_UNSUPPORTED. Query head j reads KV head j / (Hq / Hkv); the
- * scale is 1 / sqrt(D). `out` is in the activation dtype and must not overlap
- * q or the drafted rows (KV_ERR_INVALID_ARG); `lse_or_null`
- * [B, Hq, n] fp32 receives the natural-log softmax denominators. A query
- * that sees nothing gets a row of zeros and lse -inf. Keys, values and
- * queries enter the products in f16 (f16 range; each value rounded once),
- * the weights in f16, every sum in fp32.
+ * scale is 1 / sqrt(D). `out` is in the activation dtype; `lse_or_null`
+ * [B, Hq, n] fp32 receives the natural-log softmax denominators. out, lse and
+ * the workspace must not overlap one another, anything the call reads or the
+ * cache's own memory (KV_ERR_INVALID_ARG). A query that sees nothing gets a
+ * row of zeros and lse -inf. Keys, values and queries enter the products in
+ * f16 (f16 range; each value rounded once), the weights in f16, every sum in
+ * fp32.
  * Workspace: at least kv_attn_workspace_bytes(cache, n) bytes of device
  * memory, 256-byte aligned, given by the caller; nothing in it needs
  * clearing, and calls that may overlap on the GPU need one each.
