@@ -18,6 +18,7 @@
 // exchange between lanes; the norm's sum crosses the row's lanes in shuffles.
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cmath>
 #include <new>
 #include <string>
@@ -279,6 +280,21 @@ RowsDev rows_dev(const kv_rows* r) {
   return RowsDev{static_cast<uint16_t*>(r->data), r->stride_b, r->stride_h, r->stride_t};
 }
 
+// SMs of the current device, asked for once per device.
+cudaError_t sm_count(int* n) {
+  constexpr int kMaxDevices = 64;
+  static std::atomic<int> known[kMaxDevices] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < kMaxDevices && (*n = known[dev].load(std::memory_order_relaxed)) > 0) return cudaSuccess;
+  e = cudaDeviceGetAttribute(n, cudaDevAttrMultiProcessorCount, dev);
+  if (e == cudaSuccess && dev < kMaxDevices) known[dev].store(*n, std::memory_order_relaxed);
+  return e;
+}
+
+constexpr int kFillCtas = 4;  // CTAs on every SM that the launch should come to
+
 // Launch over queries and keys (H[1] = 0: one tensor).
 kv_status run_rope(const kv_rope* rope, kv_dtype dtype, int64_t batch, RopeArgs& a, bool norm, void* stream) {
   const kv_rope_config& c = rope->cfg;
@@ -295,9 +311,12 @@ kv_status run_rope(const kv_rope* rope, kv_dtype dtype, int64_t batch, RopeArgs&
   if (blocks > 0x7fffffff) return fail(KV_ERR_INVALID_ARG, "batch * n_tokens too large");
   // one warp takes all of a token's heads where there are tokens enough to
   // fill the GPU, else as few as one pass
+  int sms = 0;
+  const cudaError_t asked = sm_count(&sms);
+  if (asked != cudaSuccess) return fail(KV_ERR_CUDA, std::string("SM count: ") + cudaGetErrorString(asked));
   int split = 1;
   const int passes = (n_heads + rpp - 1) / rpp;
-  while (split < passes && blocks * split < 152 * 4) ++split;
+  while (split < passes && blocks * split < sms * kFillCtas) ++split;
   if (split > 65535) split = 65535;
   const int per = (passes + split - 1) / split;
   a.heads_per_warp = per * rpp;
