@@ -363,12 +363,11 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
               const int j = __ffs(left) - 1;
               const size_t at = ((static_cast<size_t>(b) * a.geo.H + h) * a.T + kGroup * k + j) * D + col;
               const uint16_t x = a.vd[at];
-              if ((x & 0x7fffu) < a.v_top) continue;
+              const float y = act_to_float(x, a.geo.act_bf16) * INFINITY;
 #pragma unroll
               for (int i = 0; i < 8; ++i) {
                 const int r = n + i;
-                if (r < a.rows && (draft_bits(a, b, r % a.T, k) >> j & 1u))
-                  o[i] = fmaf(act_to_float(x, a.geo.act_bf16), INFINITY, o[i]);
+                if ((x & 0x7fffu) >= a.v_top && r < a.rows && (draft_bits(a, b, r % a.T, k) >> j & 1u)) o[i] += y;
               }
             }
           }
