@@ -532,8 +532,8 @@ void plan_rows(const kv_cache* c, int n_queries, MultiPlan* p) {
   a.row_tiles = (a.rows + a.tile_rows - 1) / a.tile_rows;
   a.copies = a.tile_rows == 64 ? 2 : 1;
   p->units = static_cast<int64_t>(g.B) * g.H * a.row_tiles;
-  // at most one partial per CTA and one more per unit boundary
-  const size_t parts = static_cast<size_t>(c->sm_count + p->units);
+  // (kvq_internal.h MultiAttnArgs::part_o)
+  const size_t parts = static_cast<size_t>(c->sm_count) + static_cast<size_t>(std::min<int64_t>(p->units, c->sm_count));
   p->o_bytes = align256(parts * a.copies * a.tile_rows * g.D * 4);
   p->bytes = p->o_bytes + align256(parts * a.copies * a.tile_rows * 2 * 4);
 }
@@ -619,6 +619,7 @@ kv_status plan_multi(const kv_cache* c, int layer, const void* q, int n_queries,
   const int64_t per_unit = static_cast<int64_t>(a.n_groups) + (a.n_sink > 0) + a.tail_blocks + a.draft_blocks;
   a.lens = lens;
   a.n_ctas = kvq::multi_attn_ctas(p->units, per_unit, a.tile_rows > 32, lens != nullptr, c->sm_count);
+  a.cuts = p->units > a.n_ctas;
   // (never a whole share: a CTA with nothing but a lead would idle)
   a.seg_cost = static_cast<int>(std::min<int64_t>(kvq::multi_seg_cost(a.tile_rows), a.n_ctas > 0 ? p->units * per_unit / a.n_ctas : 0));
   if (p->units * (per_unit + a.seg_cost) >= (int64_t{1} << 31)) return fail(KV_ERR_UNSUPPORTED, "too many blocks of 32 columns");

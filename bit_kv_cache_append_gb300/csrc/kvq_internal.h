@@ -141,8 +141,13 @@ struct MultiAttnArgs {
   const int32_t* lens;    // [B] or NULL
   uint16_t* out;          // [B][Hq][T][D]
   float* lse;             // [B][Hq][T] or NULL
-  float* part_o;          // [segment][copies][tile_rows][D], or for tiles of more than 32 rows [segment][D / 4][128][4]
-  float* part_ml;         // [segment][copies][tile_rows][2] (max in log2 units, sum)
+  // Partials of the units that the ends of shares cut, one slot per CTA and unit.
+  // A share is contiguous, so a CTA has at most two: the end of a unit that the
+  // CTA before it began (the middle too, if it does not end here) in slot
+  // [cta], and the beginning of one in slot [n_ctas + cta], or where the units
+  // are fewer than the CTAs [n_ctas + unit].
+  float* part_o;          // [slot][copies][tile_rows][D], or for tiles of more than 32 rows [slot][D / 4][128][4]
+  float* part_ml;         // [slot][copies][tile_rows][2] (max in log2 units, sum)
   int T, mask_words;
   int rows, tile_rows, row_tiles;  // gqa T, rows of a tile and the tiles
   int copies;             // times a tile of 64 rows is held in the split kernel
@@ -152,6 +157,7 @@ struct MultiAttnArgs {
   int tail_blocks, draft_blocks;
   int seg_cost;           // what a segment costs beside its blocks, in blocks
   int n_ctas;
+  bool cuts;              // more units than CTAs: most lie within a share
   float qscale;           // log2(e) / sqrt(D) / k_unit
   float k_unit, v_unit;   // keys and values are held times these (powers of two)
   float v_scale;          // 1 / v_unit

@@ -31,10 +31,6 @@ namespace {
 // queries: 191 us with 2544 blocks, 187 with 477).
 constexpr int kMultiMergeWarps = 8;
 
-__host__ __device__ __forceinline__ bool by_cuts(const MultiAttnArgs& a) {
-  return a.geo.B * a.geo.H * a.row_tiles > a.n_ctas;
-}
-
 template <int D, bool WIDE>
 __global__ void __launch_bounds__(kMultiMergeWarps * 32, 4)
     multi_merge_kernel(const __grid_constant__ MultiAttnArgs a, int items, int share) {
@@ -46,7 +42,7 @@ __global__ void __launch_bounds__(kMultiMergeWarps * 32, 4)
   // sequence, unit in it, its first item, the unit's blocks, the CTAs that had some
   int b = 0, in = 0, first = 0, nb = 0, c0 = 0, c1 = -1;
   const int x = blockIdx.x;
-  const bool cuts = by_cuts(a);
+  const bool cuts = a.cuts;
   bool mine = true;
   if (!cuts) {
     b = x / per;
@@ -75,7 +71,7 @@ __global__ void __launch_bounds__(kMultiMergeWarps * 32, 4)
   }
   pdl_wait_primary();  // the partials are complete and visible from here on
   if (!mine) return;
-  const int u = b * per + in, stride = a.copies * a.tile_rows;
+  const int begin = partial_slot(a, c0, b * per + in, true), stride = a.copies * a.tile_rows;
   const int twice = a.copies - 1;                 // (one copy or two)
   const int r0 = in % a.row_tiles * a.tile_rows;  // first row of the unit
 #pragma unroll 1
@@ -120,7 +116,8 @@ __global__ void __launch_bounds__(kMultiMergeWarps * 32, 4)
 #pragma unroll
         for (int k = 0; k < NC; ++k) x[i][k] = 0.0f;
         if (p < parts) {
-          const size_t slot = static_cast<size_t>(c0 + (p >> twice) + u) * stride;
+          const int c = c0 + (p >> twice);
+          const size_t slot = static_cast<size_t>(c == c0 ? begin : c) * stride;
           const int at = (p & twice) * a.tile_rows + row;
           ml[i] = reinterpret_cast<const float2*>(a.part_ml)[slot + at];
           const float* src = a.part_o + slot * D + (WIDE ? static_cast<size_t>(ch) * stride + 4 * at : at * D + ch);
@@ -196,7 +193,7 @@ cudaError_t launch_d(const MultiAttnArgs& a, cudaStream_t s, int64_t* launches) 
   // (where all sequences have one length)
   const int parts = ((a.n_ctas + units - 1) / units + 1) * a.copies;
   const int share = parts <= 4 ? 1 : parts <= 8 ? 2 : parts <= 16 ? 4 : kMultiMergeWarps;
-  const int across = by_cuts(a) ? a.n_ctas - 1 + a.geo.B : units;
+  const int across = a.cuts ? a.n_ctas - 1 + a.geo.B : units;
   const int down = (items * share + kMultiMergeWarps - 1) / kMultiMergeWarps, fill = 4 * a.n_ctas / across;
   const dim3 grid(static_cast<unsigned>(across), static_cast<unsigned>(down < fill ? down : fill > 1 ? fill : 1));
   // scheduled as the split kernel drains (programmatic dependent launch)

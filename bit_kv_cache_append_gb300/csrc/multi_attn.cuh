@@ -136,6 +136,11 @@ struct Shares {
   }
 };
 
+// Slot of a CTA's partial of a unit (kvq_internal.h): whether it begins the unit.
+__device__ __forceinline__ int partial_slot(const MultiAttnArgs& a, int cta, int unit, bool begins) {
+  return begins ? a.n_ctas + (a.cuts ? cta : unit) : cta;
+}
+
 // Walks a CTA's share [i0, i1) of the list one segment (the blocks of a unit
 // inside the share) at a time.
 struct SegmentCursor {
@@ -176,7 +181,7 @@ struct SegmentCursor {
       if (blk0 == blk1) continue;  // only the unit's lead
       h = static_cast<int>(u / static_cast<unsigned>(a.row_tiles));
       rt = static_cast<int>(u) - h * a.row_tiles;
-      slot = cta + (b * a.geo.H + h) * a.row_tiles + rt;
+      slot = partial_slot(a, cta, (b * a.geo.H + h) * a.row_tiles + rt, blk0 == 0);
       return true;
     }
     return false;
