@@ -44,8 +44,9 @@ namespace narrow {
 // What bounds it: instruction issue (some 4000 warp instructions a tile at
 // D = 128, three quarters of them dequantisation), and fetching them: every
 // role's loop body is longer than a scheduler's instruction cache. 16
-// sequences of 32768 tokens, 32 rows a head, K2/V4: 198 us (546 MB, 2.8 TB/s);
-// four of 131072, 12 rows, K2/V2: 142 us (403 MB, 2.8 TB/s).
+// sequences of 32768 tokens, 32 rows a head, K2/V4: 198 us on the device (546 MB,
+// 2.8 TB/s); four of 131072, 12 rows, K2/V2: 142 us (403 MB, 2.8 TB/s). The
+// compiler spills 208 to 312 bytes a thread in every instance.
 //
 // Every wait is bounded; a role that gives up raises the CTA's abort flag,
 // the others leave at their next wait, and the softmax warps leave together

@@ -44,10 +44,10 @@ namespace wide {
 // What bounds it: the instruction issue of dequantisation and softmax
 // together, then shared memory (per tile 64 KB written and 96 KB read by the
 // products), then the tensor cores (1024 cycles a tile at D = 128).
-// Those 64 sequences take 155 us (321 MB, 2.1 TB/s), eight of up to 4001 tokens
-// with 1536 rows a head 186 us (101 GFLOP, 0.54 PFLOP/s); some 5 us of a segment
-// are its queries and its output, in which dequantisation is two tiles ahead at
-// most.
+// Those 64 sequences take 155 us on the device (321 MB, 2.1 TB/s), eight of up
+// to 4001 tokens with 1536 rows a head 188 us (101 GFLOP, 0.54 PFLOP/s); some
+// 5 us of a segment are its queries and its output, in which dequantisation is
+// two tiles ahead at most.
 //
 // Every wait is bounded, as in multi_narrow.cuh.
 constexpr int kSoftmaxWarps = 8, kValueWarp = 16, kScoreWarp = 24, kOutWarp = 25, kCopyWarp = 26;

@@ -269,8 +269,9 @@ kv_status kv_decode_attn_noalloc(kv_cache* cache, int layer, const void* q, floa
  * the workspace must not overlap one another, anything the call reads or the
  * cache's own memory (KV_ERR_INVALID_ARG). A query that sees nothing gets a
  * row of zeros and lse -inf. Keys, values and queries enter the products in
- * f16 (f16 range; each value rounded once), the weights in f16, every sum in
- * fp32.
+ * f16 (f16 range; each value rounded once, an exact key or value to 2^-11 of
+ * itself or to 2^-25, 2^-24 and 2^-22 with 2- and 3-bit codes, whichever is
+ * more), the weights in f16, every sum in fp32.
  * Workspace: at least kv_attn_workspace_bytes(cache, n) bytes of device
  * memory, 256-byte aligned, given by the caller; nothing in it needs
  * clearing, and calls that may overlap on the GPU need one each.
